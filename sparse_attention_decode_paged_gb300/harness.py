@@ -4,6 +4,8 @@ step.  PyTorch is used here only for device memory, streams and CUDA graphs.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -20,6 +22,16 @@ def to_device(a: np.ndarray | None, device="cuda", kind: str = "raw"):
     else:
         t = torch.from_numpy(a).to(device)
     return t
+
+
+def on_stream(stream):
+    """Context in which torch works on `stream` as the calls here take it: a
+    torch stream, a raw handle, or None for the current stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 DEVICE_ROW_KEYS = ("row_req", "row_len", "block_first", "block_nrows")
@@ -148,10 +160,12 @@ class PagePool:
     def update(self, req_from=None, req_add=None, stream=None):
         """New slot b continues old slot req_from[b] (-1: none) with room for
         req_add[b] more tokens; int sequences, or None for what the device
-        buffers hold."""
-        for buf, new in ((self.req_from, req_from), (self.req_add, req_add)):
-            if new is not None:
-                buf.copy_(torch.as_tensor(np.ascontiguousarray(new, dtype=np.int32)))
+        buffers hold.  Everything runs on `stream`: the buffers' new values
+        arrive behind the updates queued there, which read the old ones."""
+        with on_stream(stream):
+            for buf, new in ((self.req_from, req_from), (self.req_add, req_add)):
+                if new is not None:
+                    buf.copy_(torch.as_tensor(np.ascontiguousarray(new, dtype=np.int32)))
         dsa.dsa_update_pages(self.cfg, self.args, self.workspace, stream)
 
     def compact(self, stream=None):
