@@ -94,6 +94,9 @@ class DeviceStep:
         self.workspace = dsa.alloc_workspace(self.cfg, device)
         self.views = dsa.workspace_views(self.cfg, self.workspace)
         self.args = dsa.make_step_args(self.cfg, t)
+        # filled here, like every other buffer, so that no call's stream has to wait for it
+        self.dense_workspace = torch.zeros(dsa.dsa_dense_workspace_size(self.cfg), dtype=torch.uint8,
+                                           device=self.workspace.device)
 
     def step(self, stream=None):
         dsa.dsa_step(self.cfg, self.args, self.workspace, stream)
@@ -101,9 +104,6 @@ class DeviceStep:
     def dense(self, window: int = 0, sinks: int = 0, stream=None):
         """The same rows over their whole prefix, or a sliding window with
         sinks, into t["out"] and t["lse"]: a layer that selects no keys."""
-        if not hasattr(self, "dense_workspace"):
-            self.dense_workspace = torch.zeros(dsa.dsa_dense_workspace_size(self.cfg), dtype=torch.uint8,
-                                               device=self.workspace.device)
         dsa.dsa_dense_attn(self.cfg, self.t, self.dense_workspace, stream, window=window, sinks=sinks)
 
     def append(self, k_new, v_new, key_new, stream=None):

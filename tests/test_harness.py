@@ -89,3 +89,96 @@ def test_updates_in_a_row_on_a_busy_stream(handle, dsa_lib, cuda_ok):
     assert pool.req_len.tolist() == want.len and pool.page_refs.tolist() == want.refs
     live = torch.tensor(want.refs, device="cuda") > 0
     assert torch.equal(caches[0][live], expect[live]) and pool.status() == 0
+
+
+# ----------------------------------------------------------------------------
+# DeviceStep.dense and DeviceStep.append
+# ----------------------------------------------------------------------------
+@pytest.fixture
+def cpu_step(dsa_lib, monkeypatch):
+    """A DeviceStep without a GPU: (step, log of dense calls)."""
+    from sparse_attention_decode_paged_gb300 import harness, workloads
+
+    log = []
+    monkeypatch.setattr(dsa_lib, "make_step_args", lambda cfg, t: None)
+    monkeypatch.setattr(dsa_lib, "dsa_dense_attn", lambda cfg, args, ws, stream=None, window=0, sinks=0:
+                        log.append((ws, stream, window, sinks)))
+    return harness.DeviceStep(workloads.generate(1), device="cpu"), log
+
+
+def test_dense_workspace_is_there_before_the_call(cpu_step, dsa_lib, monkeypatch):
+    """Nothing is allocated or filled while dense() runs: a fill would be on another stream than the call."""
+    step, log = cpu_step
+
+    def refuse(*a, **kw):
+        raise AssertionError("a fill inside the call")
+
+    monkeypatch.setattr(torch, "zeros", refuse)
+    s = _Stream()
+    step.dense(7, 2, stream=s)
+    (ws, stream, window, sinks), = log
+    assert ws.numel() == dsa_lib.dsa_dense_workspace_size(step.cfg) and not ws.any()
+    assert stream is s and (window, sinks) == (7, 2)
+
+
+def _dense_rows_match(step, window, sinks, rows=None):
+    """step.t's outputs against the oracle on the workload's caches, at test_dense_attn's bound."""
+    from oracle import dsa_oracle as O
+    from tests.test_dense_attn import ONE_TERM, _check_row
+
+    torch.cuda.synchronize()
+    cfg, t = step.cfg, step.t
+    out, lse = t["out"].double().cpu().numpy(), t["lse"].double().cpu().numpy()
+    q, k, v = (t[n].double().cpu().numpy() for n in ("q", "k_cache", "v_cache"))
+    table = t["page_table"].cpu().numpy()
+    for r in rows if rows is not None else range(step.rows["num_rows"]):
+        n, b = int(step.rows["row_len"][r]), int(step.rows["row_req"][r])
+        pages = table[b, :-(-n // cfg.page_size)]
+        kr, vr = (c[pages].reshape(-1, *c.shape[2:])[:n] for c in (k, v))
+        _check_row(out[r], lse[r], *O.dense_row(q[r], kr, vr, cfg.sm_scale, cfg.num_kv_heads, window, sinks), n,
+                   ONE_TERM, r)
+    pad = step.rows["num_rows"]
+    assert not out[pad:].any() and np.all(lse[pad:] == -np.inf)
+
+
+@pytest.mark.gpu
+def test_dense_on_a_side_stream(dsa_lib, cuda_ok):
+    """The first call of a step's dense layer on a stream of the caller's, while the current stream is busy."""
+    from sparse_attention_decode_paged_gb300 import harness, workloads
+
+    step = harness.DeviceStep(workloads.generate(1))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20000000)  # about 10 ms: what the call put on the current stream would come late
+    step.dense(100, 3, stream=side)
+    side.synchronize()
+    _dense_rows_match(step, 100, 3)
+    step.dense()
+    _dense_rows_match(step, 0, 0)
+    assert dsa_lib.dsa_read_device_status(step.dense_workspace) == 0
+
+
+@pytest.mark.gpu
+def test_append_of_a_step(dsa_lib, cuda_ok):
+    """A step's own rows appended: the caches hold the new tokens at the rows' positions, and dense() reads them."""
+    from sparse_attention_decode_paged_gb300 import harness, workloads
+
+    step = harness.DeviceStep(workloads.generate(1))
+    cfg, t = step.cfg, step.t
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    k, v, key = (torch.randn(cfg.max_rows, *s, generator=gen, dtype=torch.bfloat16, device="cuda")
+                 for s in ((cfg.num_kv_heads, cfg.head_dim), (cfg.num_kv_heads, cfg.head_dim), (cfg.idx_dim,)))
+    was = t["idx_cache"].clone()
+    step.append(k, v, None)
+    torch.cuda.synchronize()
+    assert torch.equal(t["idx_cache"].view(torch.int16), was.view(torch.int16))  # index keys left alone
+    step.append(k, v, key)
+    step.dense()
+    n = step.rows["num_rows"]
+    at = torch.from_numpy(step.rows["row_len"][:n].astype(np.int64)).cuda() - 1
+    req = torch.from_numpy(step.rows["row_req"][:n].astype(np.int64)).cuda()
+    pg = t["page_table"][req, at // cfg.page_size].long()
+    for cache, new in (("k_cache", k), ("v_cache", v), ("idx_cache", key)):
+        assert torch.equal(t[cache][pg, at % cfg.page_size].view(torch.int16), new[:n].view(torch.int16)), cache
+    _dense_rows_match(step, 0, 0)
+    assert step.status() == 0
