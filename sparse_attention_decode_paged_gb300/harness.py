@@ -112,7 +112,8 @@ class DeviceStep:
         dsa.dsa_append(self.cfg, dict(self.t, k_new=k_new, v_new=v_new, key_new=key_new), self.workspace, stream)
 
     def status(self) -> int:
-        return dsa.dsa_read_device_status(self.workspace)
+        """The status bits of step(), append() and dense()."""
+        return dsa.dsa_read_device_status(self.workspace) | dsa.dsa_read_device_status(self.dense_workspace)
 
     def capture(self, stream: torch.cuda.Stream | None = None) -> torch.cuda.CUDAGraph:
         """Warm up once eagerly, then capture one step into a CUDA graph."""

@@ -121,6 +121,16 @@ def test_dense_workspace_is_there_before_the_call(cpu_step, dsa_lib, monkeypatch
     assert stream is s and (window, sinks) == (7, 2)
 
 
+def test_status_holds_what_dense_flagged(cpu_step, dsa_lib, monkeypatch):
+    step, _ = cpu_step
+    monkeypatch.setattr(dsa_lib, "dsa_read_device_status", lambda ws, stream=None: int(ws[:4].view(torch.int32)))
+    assert step.status() == 0
+    step.dense_workspace[0] = dsa_lib.DSA_DEV_BAD_PAGE
+    assert step.status() == dsa_lib.DSA_DEV_BAD_PAGE
+    step.workspace[0] = dsa_lib.DSA_DEV_BAD_ROW
+    assert step.status() == dsa_lib.DSA_DEV_BAD_PAGE | dsa_lib.DSA_DEV_BAD_ROW
+
+
 def _dense_rows_match(step, window, sinks, rows=None):
     """step.t's outputs against the oracle on the workload's caches, at test_dense_attn's bound."""
     from oracle import dsa_oracle as O
@@ -155,7 +165,10 @@ def test_dense_on_a_side_stream(dsa_lib, cuda_ok):
     _dense_rows_match(step, 100, 3)
     step.dense()
     _dense_rows_match(step, 0, 0)
-    assert dsa_lib.dsa_read_device_status(step.dense_workspace) == 0
+    assert step.status() == 0
+    step.t["page_table"][0, 0] = step.cfg.num_pages
+    step.dense()
+    assert step.status() == dsa_lib.DSA_DEV_BAD_PAGE
 
 
 @pytest.mark.gpu
