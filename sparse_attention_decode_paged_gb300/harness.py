@@ -104,6 +104,9 @@ class DeviceStep:
     def dense(self, window: int = 0, sinks: int = 0, stream=None):
         """The same rows over their whole prefix, or a sliding window with
         sinks, into t["out"] and t["lse"]: a layer that selects no keys."""
+        need, have = dsa.dsa_dense_workspace_size(self.cfg), self.dense_workspace.numel()
+        if need > have:  # cfg was changed since
+            raise ValueError(f"the config needs {need} bytes of dense workspace, the step was made with {have}")
         dsa.dsa_dense_attn(self.cfg, self.t, self.dense_workspace, stream, window=window, sinks=sinks)
 
     def append(self, k_new, v_new, key_new, stream=None):

@@ -131,6 +131,17 @@ def test_status_holds_what_dense_flagged(cpu_step, dsa_lib, monkeypatch):
     assert step.status() == dsa_lib.DSA_DEV_BAD_PAGE | dsa_lib.DSA_DEV_BAD_ROW
 
 
+def test_dense_of_a_config_that_outgrew_its_workspace_is_refused(cpu_step, dsa_lib):
+    step, log = cpu_step
+    step.cfg.flags |= dsa_lib.DSA_FLAG_NO_PREFILL_GROUPS
+    step.dense()
+    step.cfg.flags &= ~dsa_lib.DSA_FLAG_NO_PREFILL_GROUPS
+    step.cfg.block_rows = 4  # prompt tiles from now on
+    with pytest.raises(ValueError, match="dense workspace"):
+        step.dense()
+    assert len(log) == 1
+
+
 def _dense_rows_match(step, window, sinks, rows=None):
     """step.t's outputs against the oracle on the workload's caches, at test_dense_attn's bound."""
     from oracle import dsa_oracle as O
