@@ -166,11 +166,22 @@ class PagePool:
         req_add[b] more tokens; int sequences, or None for what the device
         buffers hold.  Everything runs on `stream`: the buffers' new values
         arrive behind the updates queued there, which read the old ones."""
+        new = [(buf, self._slots(name, a)) for name, buf, a in
+               (("req_from", self.req_from, req_from), ("req_add", self.req_add, req_add)) if a is not None]
         with on_stream(stream):
-            for buf, new in ((self.req_from, req_from), (self.req_add, req_add)):
-                if new is not None:
-                    buf.copy_(torch.as_tensor(np.ascontiguousarray(new, dtype=np.int32)))
+            for buf, a in new:
+                buf.copy_(a)
         dsa.dsa_update_pages(self.cfg, self.args, self.workspace, stream)
+
+    def _slots(self, name, a):
+        """One int32 a request slot, from an int sequence."""
+        a = np.asarray(a)
+        if a.shape != (self.cfg.max_reqs,) or a.dtype.kind not in "iu":
+            raise ValueError(f"{name}: expected {self.cfg.max_reqs} ints, one a slot, not {a.dtype} {a.shape}")
+        a32 = np.ascontiguousarray(a, dtype=np.int32)
+        if not np.array_equal(a32, a):
+            raise ValueError(f"{name}: values outside 32 bits")
+        return torch.from_numpy(a32)
 
     def compact(self, stream=None):
         """Moves the live pages to the front of the pool."""

@@ -63,6 +63,17 @@ def test_update_copies_on_its_stream(cpu_pool):
     assert log == [("from", [0, 1, 2, 3], []), ("update", None)]
 
 
+@pytest.mark.parametrize("bad", [[1], [[0, 0, 0, 0]], 0, [0] * 5, [0.5] * 4, [True] * 4,
+                                 np.array([0, 0, 0, 2 ** 32])], ids=repr)
+@pytest.mark.parametrize("name", ["req_from", "req_add"])
+def test_update_refuses_what_is_not_an_int_a_slot(name, bad, cpu_pool):
+    """One value would be spread over all slots, a fraction or a long int cut: nothing is copied or launched."""
+    pool, log = cpu_pool
+    with pytest.raises(ValueError, match=name):
+        pool.update(**{"req_from": [0, 1, 2, 3], "req_add": [0, 0, 0, 0], name: bad})
+    assert log == []
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("handle", [False, True], ids=["stream", "raw handle"])
 def test_updates_in_a_row_on_a_busy_stream(handle, dsa_lib, cuda_ok):
