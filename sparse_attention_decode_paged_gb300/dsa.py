@@ -509,6 +509,8 @@ def dsa_dense_attn(cfg, args, workspace, stream=None, window: int = 0, sinks: in
     sinks) or a dict of tensors (with window and sinks given here)."""
     if isinstance(args, dict):
         args = make_dense_args(cfg, args, window, sinks)
+    elif window or sinks:
+        raise ValueError("window and sinks are fixed by make_dense_args when args is a dsa_dense_args_t")
     _check(_lib.dsa_dense_attn(ctypes.byref(cfg), ctypes.byref(args), _ws(workspace), _stream(stream)))
 
 

@@ -217,3 +217,10 @@ def test_append_of_a_step(dsa_lib, cuda_ok):
         assert torch.equal(t[cache][pg, at % cfg.page_size].view(torch.int16), new[:n].view(torch.int16)), cache
     _dense_rows_match(step, 0, 0)
     assert step.status() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(window=5), dict(sinks=2)], ids=repr)
+def test_packed_dense_args_fix_the_window(kw, dsa_lib):
+    """A window beside packed arguments would be passed over."""
+    with pytest.raises(ValueError, match="make_dense_args"):
+        dsa_lib.dsa_dense_attn(make_cfg(dsa_lib, Pool(4, 4, 12, 16)), dsa_lib.dsa_dense_args_t(), None, **kw)
