@@ -358,9 +358,10 @@ __global__ void __launch_bounds__(32 * (1 + kMaxKvHeads), 2) sparse_attn_kernel(
   }
   pdl_launch_dependents();
   // this CTA's items from the row metadata (not produced by the top-k, so
-  // read while the top-k still runs; with prefill groups the rows the group
-  // kernel takes are known only after the kernels before)
-  if (p.grouped != nullptr) pdl_wait();
+  // in a step read while the top-k still runs; with prefill groups the rows
+  // the group kernel takes are known only after the kernels before)
+  const bool ahead = p.grouped == nullptr && p.inputs_ready;
+  if (!ahead) pdl_wait();
   const int items = p.max_rows_attn * S;
   const int nmine = static_cast<int>(blockIdx.x) < items ? (items - 1 - static_cast<int>(blockIdx.x)) / gridDim.x + 1 : 0;
   const int ncache = min(nmine, kItemCache);
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(32 * (1 + kMaxKvHeads), 2) sparse_attn_kernel(
     *reinterpret_cast<int4 *>(item_tab + 8 * k) = make_int4(x.a, x.b, x.L, x.req);
     *reinterpret_cast<int2 *>(item_tab + 8 * k + 4) = make_int2(x.r, x.s);
   }
-  if (p.grouped == nullptr) pdl_wait();  // the selection comes from the top-k kernel
+  if (ahead) pdl_wait();  // the selection comes from the top-k kernel
   __syncthreads();
 
   const long long tok_stride = static_cast<long long>(Hkv) * D * (p.kv_interleaved ? 2 : 1);  // elements per token

@@ -468,7 +468,7 @@ dsa_status_t indexer_impl(const dsa_config_t *cfg, int32_t row_begin, int32_t ro
 }
 
 dsa_status_t topk_impl(const dsa_config_t *cfg, int32_t row_begin, int32_t row_end, const float *scores,
-                       const int32_t *row_len, int32_t *topk_idx, void *workspace, bool hist,
+                       const int32_t *row_len, int32_t *topk_idx, void *workspace, bool hist, bool in_step,
                        dsa_stream_t stream) {
   DSA_CHECK_CFG(cfg);
   if (check_window(cfg, row_begin, row_end) != DSA_OK) return DSA_ERR_INVALID_ARG;
@@ -485,6 +485,7 @@ dsa_status_t topk_impl(const dsa_config_t *cfg, int32_t row_begin, int32_t row_e
   p.topk = cfg->topk;
   p.score_width = cfg->score_width;
   p.row_lo = row_begin;
+  p.inputs_ready = in_step ? 1 : 0;
   return cuda_status(dsa::launch_topk(*cfg, p, row_end - row_begin, stream), "top-k launch");
 }
 }  // namespace
@@ -540,26 +541,26 @@ dsa_status_t dsa_topk(const dsa_config_t *cfg, const float *scores, const int32_
                       int32_t *topk_idx, void *workspace, dsa_stream_t stream) {
   const bool hist = cfg != nullptr && (cfg->flags & DSA_FLAG_TOPK_HISTOGRAM) != 0;
   return topk_impl(cfg, 0, cfg != nullptr ? cfg->max_rows : 0, scores, row_len, topk_idx, workspace, hist,
-                   stream);
+                   false, stream);
 }
 
 dsa_status_t dsa_topk_window(const dsa_config_t *cfg, int32_t row_begin, int32_t row_end,
                              const float *scores, const int32_t *row_len, int32_t *topk_idx,
                              void *workspace, dsa_stream_t stream) {
   const bool hist = cfg != nullptr && (cfg->flags & DSA_FLAG_TOPK_HISTOGRAM) != 0;
-  return topk_impl(cfg, row_begin, row_end, scores, row_len, topk_idx, workspace, hist, stream);
+  return topk_impl(cfg, row_begin, row_end, scores, row_len, topk_idx, workspace, hist, false, stream);
 }
 
 }  // extern "C"
 
 namespace {
-// The attention calls; inside dsa_step (skip_empty_rows) the rows of length
-// 0 get no split partials, since the step's merge writes their outputs
-// without reading them.
+// The attention calls; inside dsa_step (in_step) the rows of length 0 get no
+// split partials, since the step's merge writes their outputs without reading
+// them, and rows and page table are read ahead (AttnParams::inputs_ready).
 dsa_status_t attn_impl(const dsa_config_t *cfg, const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *page_table, const int32_t *row_req, const int32_t *row_len,
                        const int32_t *topk_idx, float *part_m, float *part_l, float *part_acc, void *workspace,
-                       bool skip_empty_rows, dsa_stream_t stream) {
+                       bool in_step, dsa_stream_t stream) {
   DSA_CHECK_CFG(cfg);
   DSA_CHECK_DEV_PTR(q);
   DSA_CHECK_DEV_PTR(k_cache);
@@ -600,7 +601,7 @@ dsa_status_t attn_impl(const dsa_config_t *cfg, const void *q, const void *k_cac
   p.kv_interleaved = kv_interleaved ? 1 : 0;
   p.page_shift = page_shift_of(cfg);
   p.grouped = nullptr;
-  p.skip_empty_rows = skip_empty_rows ? 1 : 0;
+  p.skip_empty_rows = p.inputs_ready = in_step ? 1 : 0;
   if (dsa::group_path_enabled(*cfg)) {
     // prefill row groups: the union, the other rows (the decode kernel leaves
     // the grouped rows alone), then the groups' tensor-core attention, whose
@@ -658,7 +659,7 @@ dsa_status_t dsa_step(const dsa_config_t *cfg, const dsa_step_args_t *a, void *w
     st = indexer_impl(cfg, lo, hi, a->q_idx, a->w, a->idx_cache, a->idx_scale, a->page_table, a->row_req,
                       a->row_len, a->block_first, a->block_nrows, scores, workspace, true, stream);
     if (st != DSA_OK) return st;
-    st = topk_impl(cfg, lo, hi, scores, a->row_len, topk_idx, workspace, true, stream);
+    st = topk_impl(cfg, lo, hi, scores, a->row_len, topk_idx, workspace, true, true, stream);
     if (st != DSA_OK) return st;
   }
   st = attn_impl(cfg, a->q, a->k_cache, a->v_cache, a->page_table, a->row_req, a->row_len, topk_idx, part_m,

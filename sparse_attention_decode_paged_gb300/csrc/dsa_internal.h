@@ -37,6 +37,7 @@ struct TopkParams {
   uint32_t *row_hist;  // [R, 4096] filled by the indexer (used, then zeroed), or null
   int32_t topk, score_width;
   int32_t row_lo;          // first row of the window; one cluster per row of it
+  int32_t inputs_ready;    // see AttnParams
 };
 
 struct AttnParams {
@@ -58,6 +59,11 @@ struct AttnParams {
   int32_t page_shift;      // log2(page_size)
   const int32_t *grouped;  // [R] 1: the row is attended by the prefill-group kernel (null: no groups)
   int32_t skip_empty_rows; // 1: rows of length 0 get no partials (the step's merge never reads them)
+  // 1: rows and page table may be read before the wait for the kernel before.
+  // So inside dsa_step: its first kernel is an ordinary launch, behind
+  // everything that wrote them.  A call of its own may follow one that does
+  // (dsa_update_pages, dsa_compact_pages write the table and lengths).
+  int32_t inputs_ready;
 };
 
 // Prefill row groups: the rows of one request in a slot of kGroupRows

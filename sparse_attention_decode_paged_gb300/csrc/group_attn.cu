@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kUnionThreads) group_union_kernel(const AttnPa
   __shared__ int s_n[kGroupRows], s_len[kGroupRows];  // each member's selected entries and length
   pdl_launch_dependents();
   const int slot = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!p.inputs_ready) pdl_wait();  // rows and table may come from the kernel before
   if (warp == 0) {
     const SlotInfo si = slot_members(p, slot, lane, true);
     if (lane == 0) {
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kUnionThreads) group_union_kernel(const AttnPa
   }
   const int32_t *pt = p.page_table + static_cast<size_t>(max(req, 0)) * p.max_pages_per_req;
   // the page of this thread's first 16 positions (an input, not the top-k's
-  // output): fetched before the wait, so the first scan does not wait on it
+  // output): in a step fetched before the wait, so the first scan does not wait on it
   constexpr int kPer = kUnionScan / kUnionThreads;
   const int pg_first = members != 0u && tid * kPer < lmax ? pt[(tid * kPer) >> p.page_shift] : -1;
   pdl_wait();  // the selection comes from the top-k kernel

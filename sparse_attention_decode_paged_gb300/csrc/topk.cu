@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1) topk_cluster_kernel(const TopkPar
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.topk;
   int32_t *out = p.topk_idx + static_cast<size_t>(r) * K;
-  int L = p.row_len[r];  // row metadata, not the indexer's output: read while it finishes
+  if (!p.inputs_ready) pdl_wait();
+  int L = p.row_len[r];  // row metadata, not the indexer's output: in a step read while it finishes
   pdl_wait();            // the scores come from the indexer kernel
   if (L < 0 || L > p.score_width) {
     if (tid == 0 && q == 0) flag_status(p.status, DSA_DEV_BAD_ROW);
@@ -550,7 +551,8 @@ __global__ void __launch_bounds__(kThreads, 1) topk_stream_kernel(const TopkPara
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.topk;
   int32_t *out = p.topk_idx + static_cast<size_t>(r) * K;
-  int L = p.row_len[r];  // row metadata, not the indexer's output: read while it finishes
+  if (!p.inputs_ready) pdl_wait();
+  int L = p.row_len[r];  // row metadata, not the indexer's output: in a step read while it finishes
   pdl_wait();            // the scores come from the indexer kernel
   if (L < 0 || L > p.score_width) {
     if (tid == 0 && q == 0) flag_status(p.status, DSA_DEV_BAD_ROW);
