@@ -198,20 +198,24 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 
 // SM count of the current device, asked for once per device.
 cudaError_t sm_count(int *sms);
-// Lets `kernel` use `bytes` of dynamic shared memory on the current device.
-// `done` (one per kernel, static) remembers the most asked for on each device:
-// the attribute is a property of the loaded kernel, not of a call.
+// Lets `kernel`, which has no static shared memory, use `bytes` of it on the
+// current device.  The limit is a property of the loaded kernel, not of a call:
+// it is always set to all that a CTA can have, so that calls of other configs,
+// from other host threads too, never lower it under one another.  `done` (one
+// per kernel, static) remembers the devices where it is set.
+constexpr int kSmemOptIn = 227 * 1024;
 struct SmemLimit {
-  std::atomic<int> bytes[64];
+  std::atomic<bool> set[64];
 };
 template <typename... KArgs>
 inline cudaError_t allow_smem(void (*kernel)(KArgs...), int bytes, SmemLimit &done) {
+  if (bytes > kSmemOptIn) return cudaErrorInvalidValue;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && done.bytes[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done.bytes[dev].store(bytes, std::memory_order_release);
+  if (dev < 64 && done.set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOptIn);
+  if (e == cudaSuccess && dev < 64) done.set[dev].store(true, std::memory_order_release);
   return e;
 }
 
