@@ -2,9 +2,7 @@
 // prompt tiles (dense_prompt.cu).
 #pragma once
 
-#include <cudaTypedefs.h>
 
-#include <mutex>
 
 #include "dsa_common.cuh"
 #include "tc_ptx.cuh"
@@ -58,19 +56,5 @@ struct Shares {
 // begins in it and goes on up to CTA `last`; (-2 - id, first | last << 16) where
 // the whole share lies inside one that begins in CTA `first`; (-1, 0) else.
 __device__ __forceinline__ int2 tail_inside(int id, int first, int last) { return make_int2(-2 - id, first | last << 16); }
-
-inline PFN_cuTensorMapEncodeTiled_v12000 dense_tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
 
 }  // namespace dsa

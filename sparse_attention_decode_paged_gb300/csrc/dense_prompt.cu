@@ -987,7 +987,7 @@ template <int D>
 cudaError_t launch_prompt(const dsa_config_t &cfg, const DenseParams &p, const DensePromptParams &t,
                           const DenseLayout &rows, size_t rows_smem, const CUtensorMap (&row_maps)[2],
                           const void *k_cache, const void *v_cache, cudaStream_t st) {
-  auto encode = dense_tensor_map_encoder();
+  auto encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   constexpr uint32_t kTileB = kPT * D * 2u;
   PromptLayout lay;

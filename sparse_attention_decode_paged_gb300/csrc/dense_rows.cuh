@@ -567,7 +567,7 @@ inline size_t rows_layout(const dsa_config_t &cfg, bool listed, DenseLayout &lay
 // Tensor maps of K and V for attend_rows.
 inline cudaError_t rows_maps(const dsa_config_t &cfg, const DenseLayout &lay, const void *k_cache, const void *v_cache,
                              CUtensorMap (&maps)[2]) {
-  auto encode = dense_tensor_map_encoder();
+  auto encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   const int Hkv = cfg.num_kv_heads, D = cfg.head_dim;
   // K and V as [columns of 64 elements][tokens of the pool][64]; one box is

@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
 #include <string>
 
 #include "dsa_internal.h"
@@ -215,6 +216,39 @@ dsa_status_t set_error(dsa_status_t st, const char *fmt, ...) {
   va_end(ap);
   g_last_error = buf;
   return st;
+}
+
+namespace {
+PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
+
+CUresult CUDAAPI encode_tiled(CUtensorMap *map, CUtensorMapDataType type, cuuint32_t rank, void *base,
+                              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                              const cuuint32_t *element_strides, CUtensorMapInterleave interleave,
+                              CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                              CUtensorMapFloatOOBfill fill) {
+  auto encode = [&] {
+    return g_encode_tiled(map, type, rank, base, dims, strides, box, element_strides, interleave, swizzle, promotion,
+                          fill);
+  };
+  CUresult r = encode();
+  int dev = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+    r = encode();  // the device's context is bound to this thread now
+  return r;
+}
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  });
+  return g_encode_tiled != nullptr ? encode_tiled : nullptr;
 }
 
 cudaError_t sm_count(int *sms) {

@@ -1,6 +1,7 @@
 // Internal interface between the C-ABI layer (dsa_api.cpp) and the kernels.
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -195,6 +196,11 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   lc.numAttrs = n;
   return cudaLaunchKernelEx(&lc, kernel, args...);
 }
+
+// The driver's tensor-map encoder (null: none).  It works on a host thread
+// whose first call this is too: the driver's own call wants a context bound to
+// the thread, which the runtime does only in calls that need one.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // SM count of the current device, asked for once per device.
 cudaError_t sm_count(int *sms);

@@ -53,10 +53,8 @@
 // Every wait is bounded; a wait that runs out sets DSA_DEV_TIMEOUT and an
 // abort flag, the producers wait for their copies in flight and the MMA warp
 // for its MMAs before tensor memory is freed.
-#include <cudaTypedefs.h>
 
 #include <cstring>
-#include <mutex>
 #include <type_traits>
 
 #include "dsa_common.cuh"
@@ -762,20 +760,6 @@ __global__ void __launch_bounds__(kGThreads, 1)
   if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 group_tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 }  // namespace
 
 bool group_path_enabled(const dsa_config_t &cfg) {
@@ -801,7 +785,7 @@ cudaError_t launch_group_union(const dsa_config_t &cfg, const AttnParams &p, con
 }
 
 cudaError_t launch_group_attn(const dsa_config_t &cfg, const AttnParams &p, const GroupParams &gp, cudaStream_t st) {
-  auto encode = group_tensor_map_encoder();
+  auto encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   GroupLayout lay;
   uint32_t off = 0;

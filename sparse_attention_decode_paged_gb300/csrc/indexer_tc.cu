@@ -37,10 +37,8 @@
 //  * Every wait is bounded; a wait that runs out sets DSA_DEV_TIMEOUT and an
 //    abort flag that releases the other roles, the producer waits for its
 //    copies in flight and the MMA warp for its MMAs, and TMEM is freed.
-#include <cudaTypedefs.h>
 
 #include <cstring>
-#include <mutex>
 
 #include "dsa_common.cuh"
 #include "tc_ptx.cuh"
@@ -796,20 +794,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
