@@ -598,13 +598,15 @@ cudaError_t launch_sparse_attn(const dsa_config_t &cfg, const AttnParams &p, cud
   const int items = cfg.max_rows * cfg.num_splits;
   if (cfg.head_dim == 128) {
     auto k = sparse_attn_kernel<128>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess) return e;
+    static SmemLimit limit;
+    if ((e = allow_smem(k, static_cast<int>(smem), limit)) != cudaSuccess) return e;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem)) != cudaSuccess) return e;
     const int grid = std::max(1, std::min(items, std::max(1, per_sm) * sms));
     if ((e = launch_pdl(k, dim3(grid), dim3(threads), smem, st, 1u, p, lay)) != cudaSuccess) return e;
   } else if (cfg.head_dim == 64) {
     auto k = sparse_attn_kernel<64>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))) != cudaSuccess) return e;
+    static SmemLimit limit;
+    if ((e = allow_smem(k, static_cast<int>(smem), limit)) != cudaSuccess) return e;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, threads, smem)) != cudaSuccess) return e;
     const int grid = std::max(1, std::min(items, std::max(1, per_sm) * sms));
     if ((e = launch_pdl(k, dim3(grid), dim3(threads), smem, st, 1u, p, lay)) != cudaSuccess) return e;

@@ -892,8 +892,8 @@ cudaError_t launch_tc(const dsa_config_t &cfg, const IndexerParams &p, cudaStrea
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (cr != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(indexer_tc_kernel<RB, ATOMS, F8>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static SmemLimit limit;
+  cudaError_t e = allow_smem(indexer_tc_kernel<RB, ATOMS, F8>, static_cast<int>(smem), limit);
   if (e != cudaSuccess) return e;
   const int grid = ctas_per_sm * sm_count();
   if (grid <= 0) return cudaErrorNoDevice;
