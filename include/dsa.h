@@ -36,6 +36,8 @@
  *    never synchronize, never read device memory on the host and never
  *    allocate, so they may be captured into a CUDA graph once the library
  *    has been called once on the device outside capture.
+ *  - Host threads may call at the same time, each on a workspace of its own
+ *    (dsa_step_noalloc has one for all: see there).
  *  - Errors the host can see (bad config, NULL or misaligned pointers)
  *    return a status before anything is launched; the text of the last
  *    error is available from dsa_last_error().  Errors only the device can
@@ -479,10 +481,13 @@ dsa_status_t dsa_dense_workspace_size(const dsa_config_t *cfg, size_t *bytes);
  * left out, a row out of range sets DSA_DEV_BAD_ROW and counts as a pad row.
  * Pad rows and rows without a finite score get out = 0 and lse = -inf.  What
  * masked positions hold (infinities, NaN) does not reach a row that does not
- * see them.  The config's topk, num_splits and indexer fields are not used:
- * the work is split evenly over the GPU's SMs whatever the lengths.  The
- * result is deterministic; how a row is split, and so its last bits, follow
- * from the lengths of all rows.
+ * see them.  Of visible ones a score of -inf has no weight, a NaN or +inf score
+ * makes its head's outputs NaN and its lse not finite, and a value that is not
+ * finite makes its element of the output so (an infinity may give NaN: the
+ * probability enters as terms of either sign).  The config's topk, num_splits
+ * and indexer fields are not used: the work is split evenly over the GPU's SMs
+ * whatever the lengths.  The result is deterministic; how a row is split, and
+ * so its last bits, follow from the lengths of all rows.
  *
  * Prompt rows: with block_rows > 1 (and without DSA_FLAG_NO_PREFILL_GROUPS)
  * consecutive rows of one request, two or more, are taken together on the
@@ -490,8 +495,11 @@ dsa_status_t dsa_dense_workspace_size(const dsa_config_t *cfg, size_t *bytes);
  * rows (G query heads per KV head), unless all such rows together read less
  * than 32 MB row by row.  There each probability is rounded to bf16 before the
  * value product (the sum takes it unrounded); elsewhere it enters as two bf16
- * terms whose sum is the fp32 value to about 2^-17.  Rows may come in any
- * order; runs of rows of one request are what tiles are made of.
+ * terms whose sum is the fp32 value to about 2^-17 (DSA_FLAG_NO_PREFILL_GROUPS
+ * gives all rows that).  Rows may come in any order; runs of rows of one
+ * request are what tiles are made of.  A row of a tile with an output that is
+ * not finite is attended again, whole, by one CTA: an infinity in a prefix that
+ * 512 rows share makes the call some 15 times as long.
  *
  * One launch (rows short enough never to be split: at most 256 KB of K and V
  * at score_width), two, or four (a config with prompt rows);

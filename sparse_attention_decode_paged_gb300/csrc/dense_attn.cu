@@ -28,9 +28,9 @@
 // Bound: HBM.  4 Hkv D bytes and 4 Hq D flops per position: at 8 query heads
 // per KV head 8 flops a byte, far under what mma.sync sustains.  64 rows of
 // 32768 keys, 8 KV heads, D = 128: 1224-1248 us, 6.9-7.0 TB/s; 16 rows of
-// 1024 to 131072 keys: 634-646 us, 6.7-6.9 TB/s; 64 rows under a window of 4096:
-// 163 us, 6.3 TB/s.  A call on two short rows takes 6.1 us: one launch, one CTA
-// a row.
+// 1024 to 131072 keys: 632-649 us, 6.7-6.9 TB/s; 64 rows under a window of 4096:
+// 162-165 us, 6.2-6.3 TB/s.  A call on two short rows takes 6.1-6.2 us: one
+// launch, one CTA a row.
 #include <algorithm>
 #include <type_traits>
 

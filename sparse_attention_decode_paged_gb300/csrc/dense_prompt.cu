@@ -27,20 +27,24 @@
 //    2^8, then O_w is rescaled), p = 2^(x - m), sum in fp32, P to tensor
 //    memory over S; outputs go through shared memory in whole lines.
 // P is rounded to bf16 here (the sum l takes it unrounded): its error is that
-// of the output's own rounding, relative 2^-8 a term at most, while a second term as
-// in the per-row kernel would add a half to the tensor work.  A masked
-// position has p = 0, and 0 times an infinity or NaN in V would reach rows
-// that do not see it: V rows past the chunk's longest length are zeroed in
+// of the output's own rounding, relative 2^-8 a term at most (against 64 bits
+// the outputs of a prompt are 0.0021 to 0.0023 off, 2-norm, where unrounded ones
+// are 0.0016 to 0.0017).  A second term as in the per-row kernel adds a half to
+// the tensor work and lengthens the chain: with it the windowed prompt's call
+// takes 211 us instead of 158, and 48 decode rows beside 512 tokens 593 instead
+// of 573.
+// A masked position has p = 0, and 0 times an infinity or NaN in V would reach
+// rows that do not see it: V rows past the chunk's longest length are zeroed in
 // shared memory, and a row whose output is not finite for any other reason is
 // done again by the per-row kernel, which reads visible positions only.
 //
 // What bounds it: the chain of one query tile, S -> softmax -> P V -> next S,
 // some 3,500 cycles a key tile where both query tiles' 32 products take 2,080
 // (65 cycles a 128 x 128 x 16 MMA, measured alone).  512 tokens behind 8192 with
-// 64 / 8 heads: 114-116 us, 1.25-1.28 PFLOP/s; a 4095-token prompt under a
-// window of 1024: 129 us.  Tried and no faster, by the first of these cases
-// (120 us then): two softmax warps a row 126, P in two halves 127, an issuing
-// warp a query tile 147.  Registers split by setmaxnreg: not timed, the
+// 64 / 8 heads: 114-116 us, 1.22-1.24 PFLOP/s of products that a row sees; a
+// 4095-token prompt under a window of 1024: 129 us.  Tried and no faster, by the
+// first of these cases (120 us then): two softmax warps a row 126, P in two
+// halves 127, an issuing warp a query tile 147.  Registers split by setmaxnreg: not timed, the
 // compiler spilled.
 #include <algorithm>
 
@@ -88,7 +92,11 @@ __device__ __forceinline__ int rows_per_tile(const DenseParams &p) { return 128 
 
 // Cost of n tiles of one (chunk, KV head) with 1 or 2 query tiles: a unit a
 // product pair, and kSegCost a query tile for what a segment takes besides
-// (queries to load, the pipeline to fill and drain, outputs to write).
+// (queries to load, the pipeline to fill and drain, outputs to write).  A pair
+// alone is priced at half of two by its products, though its chain is as long
+// (see above): where calls mix chunks of both kinds, those of one query tile get
+// too few CTAs (64 requests of 4 rows each behind 8192 tokens take 375 us, of
+// one row each, the same keys, 324).
 constexpr int kSegCost = 3;
 __device__ __forceinline__ int segment_cost(int n, int tiles) { return (n + kSegCost) * tiles; }
 // Shares end at segments' ends (no partial states, no join) unless that makes
@@ -109,13 +117,16 @@ constexpr long long kLeastBytes = 32 << 20;
 
 // Tiles and single rows run side by side, each on CTAs of its own, so that
 // the former's chains and the latter's reads overlap (48 rows of up to 32768
-// keys beside 512 tokens behind 8192: 521 us, one after the other 627).  Their
+// keys beside 512 tokens behind 8192: 516 to 529 us, one after the other 627; in
+// other processes 565 to 588, and why is not known).  Their
 // times, in SM cycles: a cost unit takes 1,700, and up to 800 more as the
 // single rows near HBM's rate; single rows stream 36 (D 64: 22) bytes a cycle
 // and CTA up to that rate.  Fitted, D 128, 64 / 8 heads beside the same tokens:
 // rates of 28, 32 and 42 take 724, 588 and 559 us; without the 800, 200 rows of
 // up to 4096 keys take 411 us instead of 355, and 24 rows beside 2000 tokens 934
-// instead of 894; with a flat 2,600 a unit, 8 rows take 222 instead of 185.
+// instead of 894; with a flat 2,600 a unit, 8 rows take 222 instead of 185.  A
+// unit's times are those of D 128; D 64's are some 0.8 of them (512 tokens behind
+// 8192: the call takes 106 us, 128 with D 128).
 constexpr float kTileClk = 1700.f, kTileBusyClk = 800.f, kRowRate128 = 36.f, kRowRate64 = 22.f, kMemRate = 3450.f;
 
 // ----------------------------------------------------------------- plan
