@@ -236,9 +236,11 @@ def _dev(t, name, dtypes, numel=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _ws(workspace):
+def _ws(workspace, need=0):
     if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
         raise TypeError("workspace: expected a CUDA tensor")
+    if need and workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace: {workspace.numel() * workspace.element_size()} bytes < {need} required")
     return ctypes.c_void_p(workspace.data_ptr())
 
 
@@ -511,7 +513,8 @@ def dsa_dense_attn(cfg, args, workspace, stream=None, window: int = 0, sinks: in
         args = make_dense_args(cfg, args, window, sinks)
     elif window or sinks:
         raise ValueError("window and sinks are fixed by make_dense_args when args is a dsa_dense_args_t")
-    _check(_lib.dsa_dense_attn(ctypes.byref(cfg), ctypes.byref(args), _ws(workspace), _stream(stream)))
+    ws = _ws(workspace, dsa_dense_workspace_size(cfg))
+    _check(_lib.dsa_dense_attn(ctypes.byref(cfg), ctypes.byref(args), ws, _stream(stream)))
 
 
 # ----------------------------------------------------------------------------
@@ -572,10 +575,12 @@ def make_pages_args(cfg, t: dict, caches) -> dsa_pages_args_t:
 def dsa_update_pages(cfg, args, workspace, stream=None) -> None:
     """Drops, keeps and forks requests and gives them pages.  args: a
     dsa_pages_args_t (see make_pages_args)."""
-    _check(_lib.dsa_update_pages(ctypes.byref(cfg), ctypes.byref(args), _ws(workspace), _stream(stream)))
+    ws = _ws(workspace, dsa_pages_workspace_size(cfg))
+    _check(_lib.dsa_update_pages(ctypes.byref(cfg), ctypes.byref(args), ws, _stream(stream)))
 
 
 def dsa_compact_pages(cfg, args, workspace, stream=None) -> None:
     """Moves the live pages to the front of the pool.  args: a
     dsa_pages_args_t (see make_pages_args)."""
-    _check(_lib.dsa_compact_pages(ctypes.byref(cfg), ctypes.byref(args), _ws(workspace), _stream(stream)))
+    ws = _ws(workspace, dsa_pages_workspace_size(cfg))
+    _check(_lib.dsa_compact_pages(ctypes.byref(cfg), ctypes.byref(args), ws, _stream(stream)))

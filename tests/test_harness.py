@@ -224,3 +224,23 @@ def test_packed_dense_args_fix_the_window(kw, dsa_lib):
     """A window beside packed arguments would be passed over."""
     with pytest.raises(ValueError, match="make_dense_args"):
         dsa_lib.dsa_dense_attn(make_cfg(dsa_lib, Pool(4, 4, 12, 16)), dsa_lib.dsa_dense_args_t(), None, **kw)
+
+
+class _OnGpu(torch.Tensor):
+    """Passes for a CUDA tensor where only that and its size are asked for."""
+
+    is_cuda = True
+
+
+@pytest.mark.parametrize("short", [0, 1, 16], ids=lambda n: f"{n} short")
+@pytest.mark.parametrize("call", ["dsa_dense_attn", "dsa_update_pages", "dsa_compact_pages"])
+def test_workspace_too_small_is_refused(call, short, dsa_lib):
+    """A workspace of another call (or config) is smaller than what the kernels write."""
+    cfg = make_cfg(dsa_lib, Pool(40, 40, 120, 16), rows=64, block_rows=4)
+    dense = call == "dsa_dense_attn"
+    need = (dsa_lib.dsa_dense_workspace_size if dense else dsa_lib.dsa_pages_workspace_size)(cfg)
+    args = dsa_lib.dsa_dense_args_t() if dense else dsa_lib.dsa_pages_args_t()
+    ws = torch.zeros(need - short, dtype=torch.uint8).as_subclass(_OnGpu)
+    # the arguments are empty: what is refused first tells how far the call came
+    with pytest.raises(ValueError if short else dsa_lib.DsaError, match="workspace" if short else "page_table"):
+        getattr(dsa_lib, call)(cfg, args, ws, stream=0)
